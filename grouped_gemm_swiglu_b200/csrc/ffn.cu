@@ -348,6 +348,19 @@ __device__ __forceinline__ float rcp_fast(float x) {
     return y;
 }
 
+// min and max that give NaN where either side is NaN (fminf and fmaxf give the other side): a
+// NaN gate clamped to the limit would leave the pass as an ordinary number.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // 16 lanes x 16 fp32 columns from each of two addresses, in the matrix-fragment layout:
 // thread t holds rows t/4 and t/4 + 8, columns 2 (t % 4) + {0, 1} and those + 8:
 // v[4j + 2i + e] = row t/4 + 8i, column 8j + 2 (t % 4) + e.
@@ -935,8 +948,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         float &g0 = gv[2 * e], &g1 = gv[2 * e + 1], &u0 = uv[2 * e], &u1 = uv[2 * e + 1];
                         (F2(g0, g1) * sg2).get(g0, g1);
                         (F2(u0, u1) * su2).get(u0, u1);
-                        const F2 g(fminf(g0, lim), fminf(g1, lim));
-                        const F2 u(fminf(fmaxf(u0, -lim), lim), fminf(fmaxf(u1, -lim), lim));
+                        F2 g(g0, g1), u(u0, u1);
+                        if constexpr (clamps.value) {
+                            g = F2(min_nan(g0, lim), min_nan(g1, lim));
+                            u = F2(min_nan(max_nan(u0, -lim), lim), min_nan(max_nan(u1, -lim), lim));
+                        }
                         float e0, e1, hv[2];
                         (g * n2).get(e0, e1);
                         fma2(F2(ex2_fast(e0), ex2_fast(e1)), one, one).get(e0, e1);

@@ -427,6 +427,7 @@ int moe_dropout(const void* x, const void* residual, void* out, int64_t n, int d
  *   h[r][i] = keep(r*I + i) / (1 - drop_p) * min(gate, L) sigmoid(alpha min(gate, L))
  *             * (clamp(up, -L, L) + beta)                            (dropout of the experts)
  *   y[r] = h[r] . W2[g]^T
+ * A NaN gate or up value makes h NaN, whatever the limit (a dropped element of h is 0).
  * Arguments as moe_experts, and
  *   gu [A][2I] bf16 out: gate and up before the clamp, for the backward pass (next to the limit
  *   rounded to the side on which the value lies, so that the clamp's mask survives);
