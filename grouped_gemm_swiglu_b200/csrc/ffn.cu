@@ -481,9 +481,19 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
 // asynchronous proxy (copies, st.async, operands), through tensor memory, or is a read
 // that has returned its value. With cluster-scope release and acquire in the tile ring, and
 // the publishing fence in the epilogue, the 128-expert forward pass took 358 us, 340 without.
+// The exception is `fix`, which orders rank 1's ordinary stores of zeros before the MMAs that
+// rank 0 issues over both CTAs' operands: release and acquire at cluster scope.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, PipeAbort* ab, int* status) {
     bool ok = true;
     if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, ab, status);
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    __syncwarp();
+    return ok;
+}
+
+__device__ __forceinline__ bool warp_wait_cl(uint64_t* bar, uint32_t parity, PipeAbort* ab, int* status) {
+    bool ok = true;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait_cl(bar, parity, ab, status);
     ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
     __syncwarp();
     return ok;
@@ -885,10 +895,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 if (!warp_wait(&tail[s], (parity >> s) & 1u, ab, p.status)) break;
                 zero_k_rows<C>(smem + s * C::STAGE, rows, (rows + 15) & ~15, lane);
                 if (rank == 0) {
-                    if (!warp_wait(&fix[s], (parity >> s) & 1u, ab, p.status)) break;
+                    if (!warp_wait_cl(&fix[s], (parity >> s) & 1u, ab, p.status)) break;
                     if (lane == 0) mbar_arrive(&full[s]);
                 } else if (lane == 0) {
-                    mbar_arrive_remote(lead(&fix[s]));
+                    mbar_arrive_cluster(lead(&fix[s]));
                 }
                 parity ^= 1u << s;
             }
