@@ -1052,8 +1052,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         float g0 = lo_f(gw), g1 = hi_f(gw), u0 = lo_f(uw), u1 = hi_f(uw);
                         const float r0 = g0, r1 = g1, w0 = u0, w1 = u1;
                         if (clamps.value) {
-                            g0 = fminf(g0, lim), g1 = fminf(g1, lim);
-                            u0 = fminf(fmaxf(u0, -lim), lim), u1 = fminf(fmaxf(u1, -lim), lim);
+                            g0 = min_nan(g0, lim), g1 = min_nan(g1, lim);
+                            u0 = min_nan(max_nan(u0, -lim), lim), u1 = min_nan(max_nan(u1, -lim), lim);
                         }
                         const F2 g(g0, g1), dh(dh0, dh1);
                         float e0, e1;
@@ -1064,9 +1064,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                         float dg0, dg1, du0, du1;
                         (dh * slope * fma2(F2(u0, u1), cg2, bcg2)).get(dg0, dg1);
                         (dh * gs * cu2).get(du0, du1);
+                        // NaN: of a gate, dg and du are NaN; of an up value, dg is, and du, taken only
+                        // where |u| <= L, is 0 (without a limit, too).
                         if constexpr (clamps.value) {
-                            dg0 = r0 <= lim ? dg0 : 0.f, dg1 = r1 <= lim ? dg1 : 0.f;
+                            dg0 = r0 > lim ? 0.f : dg0, dg1 = r1 > lim ? 0.f : dg1;
                             du0 = fabsf(w0) <= lim ? du0 : 0.f, du1 = fabsf(w1) <= lim ? du1 : 0.f;
+                        } else {
+                            du0 = w0 == w0 ? du0 : 0.f, du1 = w1 == w1 ? du1 : 0.f;
                         }
                         gw = pack2(dg0, dg1);
                         uw = pack2(du0, du1);

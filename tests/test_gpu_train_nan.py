@@ -1,18 +1,19 @@
-"""NaN through the feed-forward block's training calls: NaN comes out where the definition has it, with
+"""NaN and infinities through the feed-forward block's training calls: NaN comes out where the definition has it, with
 and without a limit, and everywhere else the results are those of the clean inputs."""
 import math
 
 import pytest
 import torch
 
+from tests import train_ref as R
 from tests.test_gpu_train import DEV, INF, Ffn
 
 pytestmark = pytest.mark.gpu
 NAN = math.nan
 
-# token blocks of 64, 128 and 256 rows
+# token blocks of 64, 128 and 256 rows, and weight gradients split along the rows
 SIZES = {"64": dict(sizes=[40, 0, 90], H=256, I=256), "128": dict(sizes=[300, 3, 867], H=128, I=1024),
-         "256": dict(sizes=[3990, 0, 20, 40, 1, 2, 111], H=128, I=1024)}
+         "256": dict(sizes=[3990, 0, 20, 40, 1, 2, 111], H=128, I=1024), "split": dict(sizes=[4500], H=256, I=128)}
 ACTS = [dict(limit=0.8, alpha=1.702, beta=1.0), dict(limit=7.0, p=0.25), dict(limit=INF), dict(limit=INF, p=0.25),
         dict(limits=True, scales=True)]
 ids = lambda a: "-".join(f"{k}{v}" for k, v in a.items())  # noqa: E731
@@ -24,7 +25,7 @@ def same(got, clean, nan, what):
     assert torch.equal(got[~nan], clean[~nan]), what
 
 
-@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("size", ["64", "128", "256"])
 @pytest.mark.parametrize("act", ACTS, ids=ids)
 @pytest.mark.parametrize("where", ["x", "gate row", "up row", "both infinities"])
 def test_forward_nan(size, act, where):
@@ -63,3 +64,51 @@ def test_forward_nan(size, act, where):
     assert nan_h.any()
     same(f.h, clean.h, nan_h, "h")
     same(f.y, clean.y, nan_h.any(1, keepdim=True).expand_as(f.y), "y")
+
+
+@pytest.mark.parametrize("size", list(SIZES))
+@pytest.mark.parametrize("act", ACTS, ids=ids)
+@pytest.mark.parametrize("where", ["gate", "up"])
+def test_backward_nan(size, act, where):
+    """NaN in single saved gates or ups, against the definition in 64 bits: a NaN gate makes dgate and dup NaN, a NaN up
+    value makes dgate NaN and, as it does not lie within the limits, dup 0."""
+    f = Ffn(**SIZES[size], **act, seed=32)
+    f.forward()
+    I, n = f.dims.I, f.n
+    at = [(0, 1), (17, 40), (n - 1, I - 1), (n - 30, 100), (n - 30, 101)]
+    for r, i in at:
+        f.gu[r, i], f.gu[r, I + i] = 0.125, 0.25  # the other of the two lies within every limit
+        f.gu[r, i + (I if where == "up" else 0)] = NAN
+    if f.dims.limit < INF:  # infinities beyond the limit: no gradient of their own
+        f.gu[9, 5], f.gu[9, I + 6], f.gu[9, I + 7] = INF, INF, -INF
+    got = f.backward()
+    ref = R.ffn_backward(f.dy, f.x, f.gu, f.h, f.off, f.w1, f.gs, f.us, f.limits, f.w2, f.keep, *f.act)
+    rows = torch.zeros(n, 1, dtype=torch.bool, device=DEV)
+    feat = torch.zeros(len(f.off) - 1, 2 * I, 1, dtype=torch.bool, device=DEV)
+    for r, i in at:
+        g = max(e for e in range(len(f.off) - 1) if f.off[e] <= r)
+        rows[r] = True
+        feat[g, i] = True
+        if where == "gate":
+            feat[g, I + i] = True
+    for have, (want, err), what, nan in zip(got, ref, ("dx", "dw1", "dw2"), (rows, feat, None)):
+        nan = torch.zeros_like(have, dtype=torch.bool) if nan is None else nan.expand_as(have)
+        assert torch.equal(torch.isnan(want), nan)  # the definition
+        assert torch.equal(torch.isnan(have), nan), f"{what}: {int((torch.isnan(have) != nan).sum())} of {nan.numel()} elements"
+        R.assert_within(have[~nan], want[~nan], err[~nan], what)
+
+
+@pytest.mark.parametrize("limit", [0.8, 7.0, INF])
+def test_a_diverged_pass_shows_in_every_gradient_it_reaches(limit):
+    """A NaN in a row of x or of the weights, forward and backward together."""
+    for where in ("x", "w1"):
+        f = Ffn([50, 20], 256, 128, limit=limit, seed=33)
+        (f.x[55] if where == "x" else f.w1[1, 9])[:] = NAN
+        f.forward()
+        dx, dw1, dw2 = f.backward()
+        rows = slice(55, 56) if where == "x" else slice(50, 70)
+        assert torch.isnan(f.y[rows]).all() and torch.isnan(dx[rows]).all()
+        assert torch.isnan(dw1[1] if where == "x" else dw1[1, 9]).all()
+        assert torch.isnan(dw2[1] if where == "x" else dw2[1, :, 9]).all()
+        for t in (f.y[:50], dx[:50], dw1[0], dw2[0]):
+            assert torch.isfinite(t).all()
