@@ -79,6 +79,12 @@ class MoETraining:
             raise ValueError("MoETraining: dropout needs rng, int64 [2, 2]: {seed, offset} of the experts' and the output's mask")
         return (rng[0] if self.expert_drop else None), (rng[1] if self.out_drop else None)
 
+    def _check_inputs(self, *tensors) -> None:
+        """What the routing and permuting calls, which take addresses on trust, are handed."""
+        for name, t, dtype, shape in tensors:
+            if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.w1.device):
+                raise ValueError(f"MoETraining.forward: {name} must be a contiguous {dtype} tensor of shape {shape} on {self.w1.device}")
+
     def forward(self, logits, x, residual=None, rng=None):
         """out [T,H] bf16 (plus residual where one is given), and what backward() needs. `logits` and
         the weights must still hold the same values then."""
@@ -86,10 +92,8 @@ class MoETraining:
         if T > self.max_tokens:
             raise ValueError(f"T={T} exceeds the workspace size ({self.max_tokens} tokens)")
         d = self._dims(T)
-        for name, t, dtype, shape in (("logits", logits, torch.float32, (T, d.E + d.n_sink)), ("x", x, bf, (T, d.H)),
-                                      ("residual", residual, bf, (T, d.H))):
-            if t is not None and (t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.w1.device):
-                raise ValueError(f"MoETraining.forward: {name} must be a contiguous {dtype} tensor of shape {shape} on {self.w1.device}")
+        self._check_inputs(("logits", logits, torch.float32, (T, d.E + d.n_sink)), ("x", x, bf, (T, d.H)),
+                           ("residual", residual, bf, (T, d.H)), ("router_bias", self.router_bias, torch.float32, (d.E,)))
         r_exp, r_out = self._rngs(rng)
         A, k = d.A, d.k
         with torch.cuda.device(dev):
