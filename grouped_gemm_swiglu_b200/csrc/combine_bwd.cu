@@ -11,8 +11,9 @@
 // Bound by memory: reads y and dout once, writes dy once. One CTA per token and one warp
 // per slot: a warp streams its row of y against the token's dout (which its neighbours
 // share through L1) and writes its row of dy on the way, so there is no reduction across
-// warps and the order of every sum is fixed. Measured: 4096 tokens, top-8, H 2048 in 52 us
-// (5.5 TB/s; 43.5 us at the copy rate); eight chunks in flight per lane instead of four 56 us.
+// warps and the order of every sum is fixed. Measured: 4096 tokens, top-8, H 2048 in 54 us
+// (5.3 TB/s; 43.5 us at the copy rate); eight chunks in flight per lane instead of four 56 us
+// where four took 52.
 #include <cuda_bf16.h>
 
 #include "status.cuh"

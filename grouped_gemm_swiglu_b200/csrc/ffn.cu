@@ -57,12 +57,12 @@
 // epilogue (warp w reads TMEM lanes 32 (w % 4).., and every second 16-column chunk), two
 // 256-column TMEM accumulators. Every wait is bounded (ptx.cuh).
 //
-// Measured (one B200, at the power cap, where the clock falls from 1.9 to 1.05-1.3 GHz): a
-// dense block of 8191 rows, H 4096, I 1536, in 240-262 us forward and 490-540 us backward
-// (1.2 PFLOP/s, tensor cores 83-87 % active: 530 cycles a 64-deep step where the MMAs take
-// 512); 32768 rows over 128 experts, H 2048, I 768, in 375-420 and 815-895 us (at full clock
-// 345 and 760; groups of exactly 256 rows 365 and 785); 1024 rows over 32 experts in 57-61
-// and 129-137 us (HBM: 302 MB of weights, and as much of gradients).
+// Measured (one B200; the upper figures at the power cap, where the clock falls from 1.9 to
+// 1.05-1.3 GHz): a dense block of 8191 rows, H 4096, I 1536, in 220-264 us forward and 480-548 us
+// backward (1.2 PFLOP/s, tensor cores 83-87 % active: 530 cycles a 64-deep step where the MMAs
+// take 512); 32768 rows over 128 experts, H 2048, I 768, in 357-429 and 876-933 us (of the
+// backward pass dx alone 446, dW1 alone 483, each with dh, dW2 alone 161-202); 1024 rows over 32
+// experts in 57-60 and 131-138 us (302 MB of weights read, and as much of gradients written).
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -100,13 +100,15 @@ constexpr int kFfnManyRows = 1024;   // and above which dx comes after dW1
 //   LARGE  256 token rows a block, 64 k a step in six 32 KB stages. With 128 k in three 64 KB ones
 //          the 128-expert forward pass gained 1.5 %, its backward pass lost 6 %.
 //   MID    128 rows, 128 k in four 48 KB stages (weight gradients 64 rows a step, and never split):
-//          2000 rows, H 1024, I 512 forward 24.6 us LARGE, 22.2 MID; 300 rows, H 2048, I 1024
-//          backward 38.7 and 34.6.
+//          2000 rows, H 1024, I 512 forward 24.6 us LARGE, 22.2 MID. Backward, 128-row blocks both
+//          times, 300 rows, H 2048, I 1024 took 38.7 and 34.6 (they run SMALL now: 32.3).
 //   SMALL  64 rows, 128 k in five 40 KB stages (weight gradients 64 rows a step): two experts of
 //          30 rows, H 2048, I 1024, forward 24.8 us with 64 k in ten 20 KB stages, 21.9 so.
-//          Chosen where groups average at most 32 rows (32 experts, H 2048, I 768, forward: 32
-//          rows a group 60.9 us LARGE, 57.0 SMALL; 64 rows, whose blocks then read the weights
-//          twice, 62.7 and 71.5), and where there are few tiles (ffn_block).
+//          Chosen where groups average at most 32 rows, and where there are few tiles (ffn_block).
+//          32 experts, H 2048, I 768, us LARGE and SMALL, uneven groups (beyond 64 rows a group
+//          reads its weights twice): forward, average 32 rows 58.9, 57.2; 40 rows 59.1, 57.6;
+//          48 rows 60.7, 60.9; 64 rows 61.8, 66.8; backward 136.5, 130.9; 137, 131.7; 140.5, 139.9;
+//          147, 146. So it would gain 3 % up to about 40 rows, which the bound leaves to LARGE.
 enum { LARGE, MID, SMALL };
 template <int SIZE>
 struct FfnCfg {
@@ -147,7 +149,7 @@ inline FastDiv fast_div(int64_t d) { return FastDiv{(int)d, (uint32_t)(0xFFFFFFF
 struct FfnPhase {
     int kind;
     int rt, ct;  // token phases: ct feature tiles per block; weight gradients: rt x ct tiles per group
-    int nkb;     // token phases: 64-deep steps
+    int nkb;     // token phases: steps, FfnCfg::KT deep
     FastDiv per, panel;  // tiles per part of a group (weight gradients) or block (token phases), per panel
     int base;            // weight gradients: the phase's first tile among the split_tiles of a part
 };
@@ -166,7 +168,7 @@ struct FfnDev {
     FfnPhase ph[kFfnPhases];
     int nmaps;      // the first phases have operands
     int tb_log2;    // token rows per block: 64 (SMALL), 128 or 256
-    int max_blk;    // size of `done`
+    int max_blk;    // token blocks at most (`done` has a flag for each, and more)
     int dep_total;  // arrivals that complete a token block's UP (DH) tiles
     const float* gate_scale;
     const float* up_scale;
@@ -805,7 +807,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             }
         }
         // One thread of rank 0 issues for both CTAs. Everything a step needs is ready before
-        // the loop: its four MMAs take the tensor core 512 cycles, and building descriptors
+        // the loop: four MMAs of 256 columns take the tensor core 512 cycles, and building descriptors
         // (or the whole warp waiting) in the loop took 1100.
         if (rank == 0 && lane == 0) {
             uint32_t stage = 0, phase = 0;
@@ -1407,7 +1409,7 @@ static int ffn_block(int64_t A, int G, int I, bool bwd) {
 // Token blocks at most: every group that has rows ends in one that may be part.
 static int64_t max_blocks(int64_t A, int G, int tb) { return std::min<int64_t>(A, G) + A / tb; }
 
-// Completion flags of a workspace: enough for either block size, and never fewer for more rows,
+// Completion flags of a workspace: enough for every block size, and never fewer for more rows,
 // so that a workspace serves every smaller call. Then those of split weight gradients.
 static int64_t block_flags(int64_t A, int G) { return std::min<int64_t>(A, G) + A / FfnCfg<SMALL>::TB; }
 int64_t ffn_flags(int64_t A, int G, bool bwd) { return block_flags(A, G) + (bwd ? kFfnJoined : 0); }
@@ -1516,7 +1518,9 @@ cudaError_t launch_ffn(const FfnArgs& a, cudaStream_t stream) {
     }
     // DW1 last: what it stores at the end leaves L2 after the launch (32 experts of 32 rows: 138
     // us, 148 with DX last). Groups of many rows make its tiles the longest, which would leave
-    // pairs idle at the end (one group of 8191 rows: 541 us, 517 with DX last).
+    // pairs idle at the end (one group of 8191 rows: 541 us, 517 with DX last). In between (us with
+    // DW1 last, DX last; H 2048, I 768): 8 groups of 512 rows 79.5, 82.5; of 1024 131.8, 132.7; of
+    // 2048 241-266, 236-253; 4 of 4096 295-308, 278-289.
     const bool dx_last = a.A > (int64_t)kFfnManyRows * a.G;
     for (int pass = 0; pass < 2; ++pass) {
         if (a.A > 0 && a.dx && dx_last == (pass == 1)) {

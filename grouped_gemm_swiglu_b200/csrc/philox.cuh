@@ -12,7 +12,7 @@
 namespace moe {
 
 struct DropArgs {
-    const uint64_t* rng;  // device {seed, offset}; read only when thr > 0 or scale > 1
+    const uint64_t* rng;  // device {seed, offset}; read only when `on`
     uint32_t thr;         // words below are dropped
     float scale;          // 1 / (1 - p)
     int on;               // p > 0

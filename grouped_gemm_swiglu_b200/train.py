@@ -41,12 +41,15 @@ class MoETraining:
     """A bf16 expert layer that is trained: w1 [G,2I,H] and w2 [G,H,I] belong to the caller (an
     optimiser may change them between passes), workspaces for `max_tokens` tokens to this object.
 
-    gate_scale, up_scale, limits: optional fp32 [G]; router_bias: optional fp32 [E] (it ranks
-    only and has no gradient). expert_drop drops elements of the experts' activation h,
-    out_drop elements of the layer's output before the residual sum; both draw their masks
-    from `rng` int64 [2, 2] on the device, {seed, offset} of the experts' and of the output's
-    mask, which the caller changes from pass to pass (in place, for a captured graph) and
-    leaves alone between a forward pass and its backward pass.
+    There is no autograd function: `out` has no grad_fn, whether or not an input requires a
+    gradient, and the gradients are what backward() returns.
+
+    gate_scale, up_scale, limits: optional fp32 [G]; router_bias: optional fp32 [E] (sigmoid
+    scoring; it ranks only and has no gradient). expert_drop drops elements of the experts'
+    activation h, out_drop elements of the layer's output before the residual sum; both draw
+    their masks from `rng` int64 [2, 2] on the device, {seed, offset} of the experts' and of the
+    output's mask, which the caller changes from pass to pass (in place, for a captured graph)
+    and leaves alone between a forward pass and its backward pass.
 
     One pass at a time uses an object: passes that overlap on the GPU (other streams, other
     graphs) need objects of their own, which may share the weights.
