@@ -449,8 +449,8 @@ int moe_ffn_forward(const void* x_perm, const int32_t* offsets, const void* w1, 
  *   dgate = s_g[g] dh (clamp(up, -L, L) + beta) a'(gate) [gate <= L],
  *   dup   = s_u[g] dh a(gate) [-L <= up <= L]            (rounded to bf16 together)
  *   a(g) = min(g, L) s, a'(g) = s (1 + alpha min(g, L) (1 - s)), s = sigmoid(alpha min(g, L))
- *   (a NaN gate makes dgate and dup NaN; a NaN up value makes dgate NaN and dup 0, as it does not
- *   lie within [-L, L])
+ *   (a NaN gate makes dgate NaN, and dup where up lies within [-L, L]; a NaN up value makes dgate
+ *   NaN where gate <= L, and dup 0, as it does not lie within [-L, L])
  *   dx[r] = [dgate | dup] . W1[g]
  *   dw1[g] = sum_r [dgate | dup]^T x[r],  dw2[g] = sum_r dy[r]^T h[r]         (fp32 sums)
  *   dy [A][H] bf16 in; x_perm, gu, h, offsets, weights, scales, limits, drop_p and rng as in
